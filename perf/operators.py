@@ -209,8 +209,7 @@ def prepare(case, seed):
         st.q = _randn(g, (n, case["heads"], d), qdt)
         st.o = torch.empty_like(st.q)
         st.lse = torch.empty(n, case["heads"], dtype=torch.float32, device="cuda")
-        # the call leaves what stands behind a sequence's length as it was
-        st.scores_out = st.scores.clone() if case["scores"] else None
+        st.scores_out = torch.zeros_like(st.scores) if case["scores"] else None
     else:
         st.dst_table = _table(g, dst, max(dst), n_src, n_pages - n_src)
         for i in range(n_src, n_pages, 1 << 16):  # pages that the cache hands out anew
