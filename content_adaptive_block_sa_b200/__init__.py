@@ -528,15 +528,16 @@ def paged_append(cache: PagedCache, k_new, v_new, cu_new=None, scores=None, stre
 
 
 def paged_decode_desc(q, o, window: int = 0, sinks: int = 0, softmax_scale: float = 0.0,
-                      scores=None) -> _abi.sa_paged_decode_desc:
-    """Descriptor from q, o [n_seq, Hq, d] and scores (None: not accumulated)."""
+                      scores=None, keep_tail: bool = False) -> _abi.sa_paged_decode_desc:
+    """Descriptor from q, o [n_seq, Hq, d] and scores (None: not accumulated).
+    keep_tail: see sa_paged_decode_desc."""
     _need(q.dim() == 3 and q.shape == o.shape and q.dtype == o.dtype and q.stride(2) == 1
           and o.stride(2) == 1, "q and o must be [n_seq, Hq, d] of one type, head_dim contiguous")
     return _abi.sa_paged_decode_desc(
         dtype=_paged_dtype(q), num_q_heads=q.shape[1], window=window, sinks=sinks,
         accumulate=int(scores is not None), softmax_scale=softmax_scale,
         q_strides=(i64 * 2)(*q.stride()[:2]), o_strides=(i64 * 2)(*o.stride()[:2]),
-        score_strides=_score_strides(scores))
+        score_strides=_score_strides(scores), keep_tail=int(keep_tail))
 
 
 def paged_decode_workspace(cache: PagedCache, ddesc) -> torch.Tensor:
@@ -550,12 +551,14 @@ def sa_paged_decode(cache: PagedCache, ddesc, q, o, lse, scores_in, scores_out, 
 
 
 def paged_decode(cache: PagedCache, q, window: int = 0, sinks: int = 0, softmax_scale: float = 0.0,
-                 scores=None, scores_out=None, stream=None):
+                 scores=None, scores_out=None, stream=None, keep_tail: bool = True):
     """(o [n_seq, Hq, d] of q's type, lse fp32 [n_seq, Hq]): attention of one
     token per sequence over all of its cache, or over the first `sinks` and the
     last `window` positions. scores (fp32 [n_seq, Hkv, >= capacity]): each
     position's weights, summed over the heads of its group, are added to them in
-    place, or to a copy in scores_out."""
+    place; scores_out receives the sums of the positions below each sequence's
+    length instead, and behind it stays as it was, or with keep_tail False
+    receives scores too, up to the cache's capacity."""
     _need(q.dim() == 3 and q.shape[0] == cache.n_seq and q.shape[2] == cache.head_dim,
           f"q must be [{cache.n_seq}, Hq, {cache.head_dim}]")
     _need(scores is not None or scores_out is None, "scores_out needs scores")
@@ -568,7 +571,7 @@ def paged_decode(cache: PagedCache, q, window: int = 0, sinks: int = 0, softmax_
     with _alloc_on(cache.device, stream):
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        dd = paged_decode_desc(q, o, window, sinks, softmax_scale, scores)
+        dd = paged_decode_desc(q, o, window, sinks, softmax_scale, scores, keep_tail)
         ws = paged_decode_workspace(cache, dd)
     sa_paged_decode(cache, dd, q, o, lse, scores, scores_out, ws, stream)
     paged_decode.last_workspace = ws

@@ -82,7 +82,7 @@ class sa_paged_append_desc(C.Structure):
 class sa_paged_decode_desc(C.Structure):
     _fields_ = [("dtype", i32), ("num_q_heads", i32), ("window", i32), ("sinks", i32),
                 ("accumulate", i32), ("softmax_scale", f32), ("q_strides", i64 * 2),
-                ("o_strides", i64 * 2), ("score_strides", i64 * 2)]
+                ("o_strides", i64 * 2), ("score_strides", i64 * 2), ("keep_tail", i32)]
 
 
 class sa_evict_desc(C.Structure):

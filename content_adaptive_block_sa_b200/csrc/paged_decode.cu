@@ -72,6 +72,7 @@ struct DecodeArgs {
   int64_t qs, qh, os, oh, scs, sch;
   int hq, rep, window, sinks, most;
   bool join_by_block;
+  bool carry;        // scores_out receives scores_in behind the lengths too
   bool q_by_2, o_by_4;  // rows of q on 4-byte, of o on 8-byte boundaries
   int col_tiles;     // tiles of query heads per key/value head
   int workers;       // blocks that are resident at once
@@ -992,7 +993,8 @@ __device__ __forceinline__ float weight(float x, float lse2) {
 
 constexpr int kWeightKeys = 4 * kThreads;  // positions of a block
 
-// Adds the weights. Grid: (stretches of positions in turn, key/value head,
+// Adds the weights, and carries over what stands behind a length where the scores
+// go to another array. Grid: (stretches of positions in turn, key/value head,
 // sequence). The lengths and the scores so far are known before the earlier kernels
 // have ended. The waiting comes before any block's end, so that the grid does not
 // end before the kernels that it follows.
@@ -1006,12 +1008,13 @@ __global__ void __launch_bounds__(kThreads) paged_weights_kernel(const __grid_co
   float* to = a.scores_out + s * a.scs + g * a.sch;
   const float* lse = a.lse + (int64_t)s * a.hq + g * a.rep;
   int j0 = blockIdx.x * kWeightKeys;
-  if (j0 >= len) {
+  const int end = a.carry ? a.c.capacity : len;
+  if (j0 >= end) {
     wait_for_earlier_kernels();
     return;
   }
 #pragma unroll 1
-  for (; j0 < len; j0 += gridDim.x * kWeightKeys) {
+  for (; j0 < end; j0 += gridDim.x * kWeightKeys) {
     float w[U], was[U];
     const float* x[U];
 #pragma unroll
@@ -1021,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads) paged_weights_kernel(const __grid_co
       const int c = j < vis.first ? j : j - vis.lo + vis.first;
       x[u] = j < len && seen ? a.logits + (((int64_t)s * a.c.hkv + g) * a.most + c) * a.rep : nullptr;
       w[u] = 0.f;
-      was[u] = j < len ? old[j] : 0.f;
+      was[u] = j < end ? old[j] : 0.f;
     }
     wait_for_earlier_kernels();
     int i = 0;
@@ -1052,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads) paged_weights_kernel(const __grid_co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * kThreads + tid;
-      if (j < len && (x[u] || old != to)) to[j] = was[u] + w[u];
+      if (j < end && (x[u] || old != to)) to[j] = was[u] + w[u];
     }
   }
 }
@@ -1144,6 +1147,7 @@ cudaError_t launch_paged_decode(const sa_paged_cache& c, const sa_paged_decode_d
   a.lse = lse;
   a.scores_in = scores_in;
   a.scores_out = scores_out;
+  a.carry = scores_in != scores_out && !d.keep_tail;
   char* base = (char*)ws;
   a.status = (DeviceStatus*)base;
   a.errors = (int32_t*)(base + plan.errors);

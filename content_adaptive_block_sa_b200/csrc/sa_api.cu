@@ -638,6 +638,7 @@ static sa_status check_paged_decode(const sa_paged_cache* c, const sa_paged_deco
   SA_CHECK(d->window >= 0 && d->sinks >= 0 && (d->window > 0 || d->sinks == 0),
            SA_ERR_INVALID_ARG);
   SA_CHECK(d->accumulate == 0 || d->accumulate == 1, SA_ERR_INVALID_ARG);
+  SA_CHECK(d->keep_tail == 0 || d->keep_tail == 1, SA_ERR_INVALID_ARG);
   SA_CHECK(d->softmax_scale >= 0.f && isfinite(d->softmax_scale), SA_ERR_INVALID_ARG);
   for (int i = 0; i < 2; ++i)
     SA_CHECK(d->q_strides[i] >= 0 && d->o_strides[i] >= 0, SA_ERR_INVALID_ARG);

@@ -604,7 +604,11 @@ sa_status sa_paged_append(const sa_paged_cache* cache, const sa_paged_append_des
  *  accumulate  1: add the attention weights to scores; 0: scores are NULL.
  *  softmax_scale  0 selects 1/sqrt(d).
  *  q_strides, o_strides  {sequence, head} element strides.
- *  score_strides  {sequence, head} element strides of scores_in and scores_out. */
+ *  score_strides  {sequence, head} element strides of scores_in and scores_out.
+ *  keep_tail   of a scores_out that is not scores_in. 0: its positions from a
+ *              sequence's length up to the capacity receive those of scores_in, so
+ *              that it is the whole array, scores_in plus the weights; 1: they stay
+ *              as they were. */
 typedef struct sa_paged_decode_desc {
   int32_t dtype;
   int32_t num_q_heads;
@@ -615,6 +619,7 @@ typedef struct sa_paged_decode_desc {
   int64_t q_strides[2];
   int64_t o_strides[2];
   int64_t score_strides[2];
+  int32_t keep_tail;
 } sa_paged_decode_desc;
 
 /* Bytes of workspace sa_paged_decode needs (with `accumulate`, 4 bytes for
@@ -630,7 +635,8 @@ sa_status sa_paged_decode_workspace_size(const sa_paged_cache* cache,
  *  scores_in, scores_out  with `accumulate`: DEVICE fp32 [n_seq, Hkv, >=
  *              capacity]; scores_out[s, g, j] = scores_in[s, g, j] + sum of
  *              exp(x_hj - LSE_h) over the query heads h of key/value head g (0
- *              where j is not visible), for j below the sequence's length. The
+ *              where j is not visible), for j below the sequence's length, and
+ *              scores_in[s, g, j] from there to the capacity (see keep_tail). The
  *              two may be the same array and must not overlap otherwise.
  * The work is split over the sequences' lengths as they are on the device, so a
  * captured call follows them. Deterministic: the same inputs give the same bits. */
