@@ -1,5 +1,6 @@
 """Paged cache operators at the edges of their contracts; bounds as in test_gpu_paged."""
 import numpy as np
+import numpy as np
 import pytest
 import torch
 
@@ -71,3 +72,59 @@ def test_a_captured_decode_carries_scores_behind_the_lengths_of_the_replay(sa):
         g.replay()
         sa.paged_decode(c.cache, q, scores=work)
         assert torch.equal(out, work)
+
+
+# ------------------------------------------- weights far below the largest
+def put_rows(c, i, s, x):
+    """Rows x [Hkv, n, d] of sequence s into the keys (0) or values (1)."""
+    x = x.to(c.k.dtype)
+    c.rows[i][s] = x
+    j = torch.arange(x.shape[1], device="cuda")
+    bits = torch.uint8 if x.dtype == TYPES["e4m3"] else torch.int16
+    pool = (c.k, c.v)[i].view(bits)
+    pool[c.table[s].long()[j // c.page], :, j % c.page] = x.cuda().view(bits).transpose(0, 1)
+
+
+@pytest.mark.parametrize("tail", ["equal", "spread"])
+@pytest.mark.parametrize("at", [0, 700])
+@pytest.mark.parametrize("cache,hq,hkv,d,n", [
+    ("fp16", 300, 300, 64, 1024), ("e4m3", 300, 300, 64, 1100), ("bf16", 300, 300, 64, 1024),
+    ("fp16", 320, 40, 128, 1500), ("e4m3", 320, 40, 128, 1500),
+    ("fp16", 480, 40, 128, 1111), ("e4m3", 480, 40, 64, 1111),
+])
+def test_one_key_far_above_the_rest_with_a_value_of_zero(sa, cache, hq, hkv, d, n, at, tail):
+    """A first key that takes almost all of the weight and gives nothing, as trained
+    models leave it: O is the sum over the rest, each of whose weights is 10 to 45
+    nats smaller (another gap for every query head), and has to be as exact
+    relative to that sum as any other."""
+    c = Case(sa, 320, [n], hkv, d, 16, cache, scales=False)
+    r = np.random.default_rng(321)
+    k = torch.zeros(hkv, n, d) if tail == "equal" else torch.tensor(r.standard_normal((hkv, n, d)) * 0.2).float()
+    k[:, at] = 4.0
+    v = torch.full((hkv, n, d), 96.0) if tail == "equal" else torch.tensor(1 + r.standard_normal((hkv, n, d))).float()
+    v[:, at] = 0.0
+    put_rows(c, 0, 0, k)
+    put_rows(c, 1, 0, v)
+    gap = torch.linspace(10, 45, hq)[torch.tensor(r.permutation(hq))]
+    q = (gap / (4 * d ** 0.5))[None, :, None].expand(1, hq, d).to(c.query(hq).dtype).contiguous().cuda()
+    before = c.scores()
+    work = before.clone()
+    o, lse = sa.paged_decode(c.cache, q, scores=work)
+    assert status(sa.paged_decode) == (0, 0)
+    check_decode(c, q, o, lse, before=before, after=work)
+
+
+@pytest.mark.parametrize("cache", ["fp16", "e4m3"])
+def test_logits_that_fall_and_rise_over_a_long_row(sa, cache):
+    """Tiles of keys whose logits step down and up by tens of nats: the running
+    maximum is raised many times, and most tiles lie far below it."""
+    n, hkv, d = 4096, 2, 64
+    c = Case(sa, 330, [n, n], hkv, d, 64, cache, scales=False)
+    r = np.random.default_rng(331)
+    level = torch.tensor(r.permutation(n // 64) / (n // 64) * 4.0).repeat_interleave(64).float()
+    for s in range(2):
+        k = torch.tensor(r.standard_normal((hkv, n, d)) * 0.05).float() + (level if s else level.sort().values)[None, :, None]
+        put_rows(c, 0, s, k)
+    q = torch.full((2, 16, d), 1.0, dtype=c.query(16).dtype, device="cuda")  # logits 0 .. 32
+    o, lse = sa.paged_decode(c.cache, q)
+    check_decode(c, q, o, lse)
