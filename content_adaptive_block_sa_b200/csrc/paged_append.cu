@@ -7,7 +7,9 @@
 //
 // One launch does it all: block 0 checks every sequence's range and pages and
 // is the only writer of the status word, so that no clearing pass is needed;
-// the other blocks skip, on their own, the rows that it reports.
+// the other blocks skip, on their own, the rows that it reports. They find a row's
+// sequence by bisection, which may miss one where the starts do not ascend; block
+// 0 sees that and then writes the rows of every valid range itself.
 #include "paged.cuh"
 
 namespace sa {
@@ -86,9 +88,11 @@ __device__ __forceinline__ uint4 quantize16(const uint4* in, float scale) {
 
 // The check of every sequence's length, range and pages, by one block: a lane
 // takes a sequence and its one or two pages, a warp the pages of a longer range.
-__device__ void check_block(const AppendArgs& a) {
+// Tells whether the ranges' starts descend anywhere.
+__device__ bool check_block(const AppendArgs& a) {
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;
+  bool descends = false;
   __syncthreads();
   const int lane = threadIdx.x & 31;
   int mine = 0;
@@ -102,6 +106,7 @@ __device__ void check_block(const AppendArgs& a) {
       int first, last;
       const bool ok = new_rows(a, s, len, &first, &last);
       if (!ok || (s == 0 && first != 0)) mine = kWherePagedRange;
+      descends |= first > last;
       if (ok && last > first) {
         p0 = (len - (last - first)) / a.c.page_size;
         np = (len - 1) / a.c.page_size - p0 + 1;
@@ -120,26 +125,79 @@ __device__ void check_block(const AppendArgs& a) {
     }
   }
   if (mine) atomicMax(&bad, mine);
-  __syncthreads();
+  descends = __syncthreads_or(descends);
   if (threadIdx.x == 0) {
     a.status->code = bad ? SA_ERR_DEVICE : SA_OK;
     a.status->where = bad;
   }
+  return descends;
 }
 
-// T: the new rows' type where the cache is e4m3; char: the cache's own type,
-// copied. A warp takes a token: one look-up, then the pieces of all its heads.
-template <typename T, int kVecs>  // kVecs: 16-byte pieces of a cache row
+// Row t of the input to position `pos` of sequence s, by a warp: one look-up, then
+// the pieces of all its heads. T: the new rows' type where the cache is e4m3; char:
+// the cache's own type, copied. kVecs: 16-byte pieces of a cache row.
+template <typename T, int kVecs>
+__device__ __forceinline__ void put_row(const AppendArgs& a, int s, int64_t t, int pos) {
+  constexpr int kIn = sizeof(T) == 1 ? 1 : 2;  // 16-byte pieces of the new row for one of the cache's
+  const int lane = threadIdx.x & 31, pieces = a.c.hkv * kVecs;
+  const int64_t at = paged_row(a.c, a.c.table + s * a.c.table_stride, pos);
+  if (at < 0) return;
+  // a copy takes two pieces of a lane at once; the quotients leave registers for one
+  constexpr int U = sizeof(T) == 1 ? 2 : 1;
+  for (int p0 = lane; p0 < pieces; p0 += 32 * U) {
+    uint4 k[U][kIn], v[U][kIn];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + 32 * u, h = p / kVecs, vec = p % kVecs;
+      if (p >= pieces) continue;
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) {
+        k[u][i] = ((const uint4*)(a.k + t * a.kst + h * a.ksh))[vec * kIn + i];
+        v[u][i] = ((const uint4*)(a.v + t * a.vst + h * a.vsh))[vec * kIn + i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + 32 * u, h = p / kVecs, vec = p % kVecs;
+      if (p >= pieces) continue;
+      const int64_t to = at + h * a.c.sh + vec * 16;
+      if constexpr (sizeof(T) == 1) {
+        *(uint4*)(a.c.k + to) = k[u][0];
+        *(uint4*)(a.c.v + to) = v[u][0];
+      } else {
+        *(uint4*)(a.c.k + to) = quantize16<T>(k[u], a.c.k_scale ? a.c.k_scale[h] : 1.f);
+        *(uint4*)(a.c.v + to) = quantize16<T>(v[u], a.c.v_scale ? a.c.v_scale[h] : 1.f);
+      }
+    }
+  }
+  if (a.scores != nullptr)
+    for (int h = lane; h < a.c.hkv; h += 32) a.scores[s * a.scs + h * a.sch + pos] = 0.f;
+}
+
+// Every valid range by one block, whatever the order of the ranges: a row that two
+// of them name goes to both. Where another block has written a row too, it wrote
+// the same. An input that is reported as bad may be slow.
+template <typename T, int kVecs>
+__device__ __noinline__ void put_every_range(const AppendArgs& a) {
+  for (int s = 0; s < a.c.n_seq; ++s) {
+    bool bad = false;
+    const int len = paged_len(a.c, s, &bad);
+    int first, last;
+    if (!new_rows(a, s, len, &first, &last)) continue;
+    for (int64_t t = first + (int)(threadIdx.x >> 5); t < last; t += kThreads / 32)
+      put_row<T, kVecs>(a, s, t, len - (last - (int)t));
+  }
+}
+
+template <typename T, int kVecs>
 __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const __grid_constant__ AppendArgs a) {
   wait_for_earlier_kernels();
   let_next_kernel_start();
   if (blockIdx.x == 0) {
-    check_block(a);
+    if (check_block(a)) put_every_range<T, kVecs>(a);
     return;
   }
   constexpr int kWarps = kThreads / 32;
-  constexpr int kIn = sizeof(T) == 1 ? 1 : 2;  // 16-byte pieces of the new row for one of the cache's
-  const int lane = threadIdx.x & 31, pieces = a.c.hkv * kVecs;
   const int step = (gridDim.x - 1) * kWarps;
   for (int64_t t = (blockIdx.x - 1) * kWarps + (threadIdx.x >> 5); t < a.n_tokens; t += step) {
     int s = (int)t;
@@ -156,39 +214,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const __grid_
     const int len = paged_len(a.c, s, &bad);
     int first, last;
     if (!new_rows(a, s, len, &first, &last) || t < first || t >= last) continue;
-    const int pos = len - (last - (int)t);
-    const int64_t at = paged_row(a.c, a.c.table + s * a.c.table_stride, pos);
-    if (at < 0) continue;
-    // a copy takes two pieces of a lane at once; the quotients leave registers for one
-    constexpr int U = sizeof(T) == 1 ? 2 : 1;
-    for (int p0 = lane; p0 < pieces; p0 += 32 * U) {
-      uint4 k[U][kIn], v[U][kIn];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int p = p0 + 32 * u, h = p / kVecs, vec = p % kVecs;
-        if (p >= pieces) continue;
-#pragma unroll
-        for (int i = 0; i < kIn; ++i) {
-          k[u][i] = ((const uint4*)(a.k + t * a.kst + h * a.ksh))[vec * kIn + i];
-          v[u][i] = ((const uint4*)(a.v + t * a.vst + h * a.vsh))[vec * kIn + i];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int p = p0 + 32 * u, h = p / kVecs, vec = p % kVecs;
-        if (p >= pieces) continue;
-        const int64_t to = at + h * a.c.sh + vec * 16;
-        if constexpr (sizeof(T) == 1) {
-          *(uint4*)(a.c.k + to) = k[u][0];
-          *(uint4*)(a.c.v + to) = v[u][0];
-        } else {
-          *(uint4*)(a.c.k + to) = quantize16<T>(k[u], a.c.k_scale ? a.c.k_scale[h] : 1.f);
-          *(uint4*)(a.c.v + to) = quantize16<T>(v[u], a.c.v_scale ? a.c.v_scale[h] : 1.f);
-        }
-      }
-    }
-    if (a.scores != nullptr)
-      for (int h = lane; h < a.c.hkv; h += 32) a.scores[s * a.scs + h * a.sch + pos] = 0.f;
+    put_row<T, kVecs>(a, s, t, len - (last - (int)t));
   }
 }
 

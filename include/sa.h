@@ -587,7 +587,8 @@ sa_status sa_paged_append_workspace_size(const sa_paged_cache* cache,
  *              cu_new[n_seq] on are ignored. NULL: row s is the one new token of
  *              sequence s (n_tokens >= n_seq; nothing for a sequence of length 0).
  *              A sequence whose range is not ascending, leaves the rows or
- *              exceeds its length is skipped and reported (SA_ERR_DEVICE).
+ *              exceeds its length is skipped and reported (SA_ERR_DEVICE); the
+ *              others are written (a row that two ranges name goes to both).
  *  scores      DEVICE fp32 [n_seq, Hkv, >= capacity] accumulated weights (see
  *              sa_paged_decode): zeroed at the new positions. NULL: none.
  * Two tokens must not name the same slot. One launch. */

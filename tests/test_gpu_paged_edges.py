@@ -1,10 +1,9 @@
 """Paged cache operators at the edges of their contracts; bounds as in test_gpu_paged."""
 import numpy as np
-import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import LOCAL, TYPES, U, Case, check_decode, half_step, new_rows, status, to_np
+from test_gpu_paged import LOCAL, TYPES, U, Case, check_decode, expect_append, half_step, new_rows, status, to_np
 
 from oracle import paged as Pg
 
@@ -128,3 +127,36 @@ def test_logits_that_fall_and_rise_over_a_long_row(sa, cache):
     q = torch.full((2, 16, d), 1.0, dtype=c.query(16).dtype, device="cuda")  # logits 0 .. 32
     o, lse = sa.paged_decode(c.cache, q)
     check_decode(c, q, o, lse)
+
+
+# ------------------------------------------------ ranges that do not ascend
+@pytest.mark.parametrize("cache,t", [("bf16", "bf16"), ("e4m3", "bf16"), ("e4m3", "fp16")])
+@pytest.mark.parametrize("cu,lens,bad", [
+    ([0, 99, 8, 12], [20, 30, 40], [0, 1]),                 # a valid range behind a start past the rows
+    ([0, 4, 2, 12], [20, 30, 40], [1]),                     # rows 2 and 3 belong to two ranges
+    ([0, 12, 3, 9, 1, 5], [20, 12, 6, 9, 7], [1, 3]),       # ranges inside another
+    ([5, 9, 2, 2, 12], [9, 9, 0, 30], [1]),                 # does not begin at row 0
+    ([0, -5, 3, 7], [3, 8, 60], [0, 1]),                    # a negative start
+    ([0, 12, 0, 12, 0, 12] * 8 + [2 ** 31 - 1, -2 ** 31, 0, 4], [33] * 51, None),
+])
+def test_append_writes_every_valid_range_whatever_their_order(sa, cu, lens, bad, cache, t):
+    c = Case(sa, 340, lens, 2, 64, 16, cache)
+    total = 12
+    valid = [0 <= a <= b <= total and b - a <= n for a, b, n in zip(cu, cu[1:], lens)]
+    assert bad is None or [s for s, ok in enumerate(valid) if not ok] == bad
+    kn, vn = new_rows(c, total, t)
+    bits = torch.uint8 if cache == "e4m3" else torch.int16
+    want = [p.view(bits).cpu().numpy().copy() for p in (c.k, c.v)]
+    scores = c.scores()
+    old = scores.clone()
+    sa.paged_append(c.cache, kn, vn, torch.tensor(cu, dtype=torch.int32).cuda(), scores)
+    assert status(sa.paged_append) == (sa.SA_ERR_DEVICE, LOCAL["where_range"])
+    for i, (x, scale) in enumerate(((kn, c.ks), (vn, c.vs))):
+        rows = expect_append(c, x, scale)
+        for s, ok in enumerate(valid):
+            for r in range(cu[s], cu[s + 1]) if ok else ():
+                j = lens[s] - (cu[s + 1] - r)
+                want[i][c.table_np[s, j // 16], :, j % 16] = rows[r]
+                old[s, :, j] = 0
+        np.testing.assert_array_equal((c.k, c.v)[i].view(bits).cpu().numpy(), want[i])
+    assert torch.equal(scores, old)
