@@ -575,10 +575,35 @@ static sa_status check_paged_cache(const sa_paged_cache* c) {
   return SA_OK;
 }
 
-// Row strides of a [n_seq, Hkv, positions] array that holds `positions` of each.
+// Whether rows of `inner` elements, `extents[i]` of them along axis i at the given
+// strides (not negative), lie apart, each axis beyond the span of the finer ones:
+// true for slices of a dense array in any order of its axes. An array that kernels
+// write must not hold an element twice.
+static bool rows_apart(const int64_t* strides, const int64_t* extents, int n, int64_t inner) {
+  __int128 span = inner;
+  bool done[3] = {};
+  for (int k = 0; k < n; ++k) {
+    int at = -1;  // the finest axis left
+    for (int i = 0; i < n; ++i)
+      if (!done[i] && (at < 0 || strides[i] < strides[at])) at = i;
+    done[at] = true;
+    if (extents[at] <= 1) continue;
+    if (strides[at] < span) return false;
+    span += (__int128)strides[at] * (extents[at] - 1);
+  }
+  return true;
+}
+
+// Strides of a [n_seq, Hkv, positions] array that holds `positions` of each.
 static bool score_strides_ok(const sa_paged_cache& c, const int64_t* s, int64_t positions) {
-  return (c.num_kv_heads == 1 || s[1] >= positions) && s[0] >= 0 && s[1] >= 0 &&
-         (c.n_seq == 1 || s[0] >= positions);
+  const int64_t extents[2] = {c.n_seq, c.num_kv_heads};
+  return s[0] >= 0 && s[1] >= 0 && rows_apart(s, extents, 2, positions);
+}
+
+// The pools of a call that writes them.
+static bool pools_apart(const sa_paged_cache& c) {
+  const int64_t extents[3] = {c.n_pages, c.num_kv_heads, c.page_size};
+  return rows_apart(c.strides, extents, 3, c.head_dim);
 }
 
 static int64_t capacity_of(const sa_paged_cache& c) { return paged_capacity(c); }
@@ -594,6 +619,7 @@ static sa_status check_paged_append(const sa_paged_cache* c, const sa_paged_appe
   if (st != SA_OK) return st;
   SA_CHECK(d != nullptr, SA_ERR_INVALID_ARG);
   SA_CHECK(d->dtype == c->dtype || beside_ok(*c, d->dtype), SA_ERR_UNSUPPORTED);
+  SA_CHECK(pools_apart(*c), SA_ERR_INVALID_ARG);
   SA_CHECK(d->n_tokens >= 0 && d->n_tokens <= kMaxCapacity, SA_ERR_INVALID_ARG);
   SA_CHECK(rows_aligned(d->k_strides, 2, dtype_bytes(d->dtype)) &&
                rows_aligned(d->v_strides, 2, dtype_bytes(d->dtype)),
@@ -664,6 +690,8 @@ sa_status sa_paged_decode(const sa_paged_cache* cache, const sa_paged_decode_des
   if (st != SA_OK) return st;
   SA_CHECK(q && o && lse && aligned(q, 2) && aligned(o, 2) && aligned(lse, 4), SA_ERR_INVALID_ARG);
   SA_CHECK(o != q, SA_ERR_INVALID_ARG);
+  const int64_t rows[2] = {cache->n_seq, desc->num_q_heads};
+  SA_CHECK(rows_apart(desc->o_strides, rows, 2, cache->head_dim), SA_ERR_INVALID_ARG);
   SA_CHECK((scores_in != nullptr) == (desc->accumulate == 1) &&
                (scores_out != nullptr) == (desc->accumulate == 1),
            SA_ERR_INVALID_ARG);
@@ -678,6 +706,7 @@ static sa_status check_evict(const sa_paged_cache* c, const sa_evict_desc* d) {
   const sa_status st = check_paged_cache(c);
   if (st != SA_OK) return st;
   SA_CHECK(d != nullptr, SA_ERR_INVALID_ARG);
+  SA_CHECK(pools_apart(*c), SA_ERR_INVALID_ARG);
   SA_CHECK(d->budget >= 1 && d->sinks >= 0 && d->recent >= 0, SA_ERR_INVALID_ARG);
   SA_CHECK((int64_t)d->sinks + d->recent <= d->budget, SA_ERR_INVALID_ARG);
   SA_CHECK(d->budget <= kMaxCapacity, SA_ERR_UNSUPPORTED);

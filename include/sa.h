@@ -527,6 +527,8 @@ sa_status sa_gist_decode_noalloc(const sa_decode_desc* desc, const void* q,
  *  strides     {page, head, position} element strides shared by k and v; the
  *              head_dim axis is contiguous. Every row starts on a 16-byte
  *              boundary (16-byte aligned pools, strides multiples of 16 bytes).
+ *              Calls that write the pools (append, eviction) refuse strides by
+ *              which rows overlap, as an expanded axis has.
  *              Pages and positions span less than 2^32 times the largest power
  *              of two that divides their strides in bytes (64 GiB at 16; 1 TiB
  *              at rows of 256 bytes side by side).
@@ -604,8 +606,11 @@ sa_status sa_paged_append(const sa_paged_cache* cache, const sa_paged_append_des
  *              and the first `sinks`; 0: it sees all (sinks is then 0).
  *  accumulate  1: add the attention weights to scores; 0: scores are NULL.
  *  softmax_scale  0 selects 1/sqrt(d).
- *  q_strides, o_strides  {sequence, head} element strides.
- *  score_strides  {sequence, head} element strides of scores_in and scores_out.
+ *  q_strides, o_strides  {sequence, head} element strides; the rows of o must not
+ *              overlap.
+ *  score_strides  {sequence, head} element strides of scores_in and scores_out;
+ *              their rows of `capacity` positions must not overlap (so in every
+ *              call with scores).
  *  keep_tail   of a scores_out that is not scores_in. 0: its positions from a
  *              sequence's length up to the capacity receive those of scores_in, so
  *              that it is the whole array, scores_in plus the weights; 1: they stay
