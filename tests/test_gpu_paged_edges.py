@@ -160,3 +160,35 @@ def test_append_writes_every_valid_range_whatever_their_order(sa, cu, lens, bad,
                 old[s, :, j] = 0
         np.testing.assert_array_equal((c.k, c.v)[i].view(bits).cpu().numpy(), want[i])
     assert torch.equal(scores, old)
+
+
+# --------------------------------------------------- offsets past 32 bits
+def test_eviction_moves_rows_past_32_bits(sa):
+    """Pages 0 and 1 are 2^32 + 4096 elements apart: rows move in place, and from
+    either page to the other, and every byte of both pools is compared."""
+    d, page, far = 128, 16, 2 ** 32 + 4096
+    flat = [torch.zeros(far + 2 * page * d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pools = [torch.as_strided(x, (2, 2, page, d), (far, page * d, d, 1)) for x in flat]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    lens = torch.empty(1, dtype=torch.int32, device="cuda")
+    for src, dst, n, budget in (([1, 0], None, 29, 20), ([0, 1], None, 32, 7), ([1], [0], 16, 9), ([0], [1], 13, 5)):
+        for x in pools:
+            x.copy_(torch.randn(2, 2, page, d, device="cuda", generator=g))
+        was = [x.clone() for x in pools]
+        scores = torch.rand(1, 2, len(src) * page, device="cuda", generator=g)
+        host = scores.cpu().numpy()
+        cache = sa.PagedCache(*pools, torch.tensor([src], dtype=torch.int32, device="cuda"), lens.fill_(n))
+        to = None if dst is None else torch.tensor([dst], dtype=torch.int32, device="cuda")
+        keep = sa.cache_evict(cache, scores, budget, 1, 2, to)
+        assert status(sa.cache_evict) == (0, 0) and lens.item() == budget
+        want = [x.clone() for x in was]
+        for h in range(2):
+            kept = Pg.keep_one(host[0, h], n, budget, 1, 2)
+            assert keep[0, h].tolist() == kept.tolist()
+            for x, y in zip(want, was):
+                for i, j in enumerate(kept.tolist()):
+                    x[(dst or src)[i // page], h, i % page] = y[src[j // page], h, j % page]
+        for x, y in zip(pools, want):
+            assert torch.equal(x, y)
+    for x in flat:  # nothing between the pages was touched
+        assert not x[2 * page * d:far].any()
