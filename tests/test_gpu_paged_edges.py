@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged import LOCAL, TYPES, U, Case, check_decode, expect_append, half_step, new_rows, status, to_np
+from test_gpu_paged import LOCAL, TYPES, Case, check_decode, expect_append, new_rows, status
 
 from oracle import paged as Pg
 
@@ -192,3 +192,56 @@ def test_eviction_moves_rows_past_32_bits(sa):
             assert torch.equal(x, y)
     for x in flat:  # nothing between the pages was touched
         assert not x[2 * page * d:far].any()
+
+
+# ------------------------------------------------------------ two streams
+def test_weights_of_calls_on_two_streams_do_not_meet(sa):
+    cs = [Case(sa, 350 + i, [700, 33, 90 + 40 * i], 2, 128, 16) for i in range(2)]
+    qs = [c.query(8) for c in cs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = []
+    for k in range(12):
+        c, q, s = cs[k % 2], qs[k % 2], streams[k % 2]
+        before = c.scores()
+        calls.append((c, q, s, before, before.clone(), torch.full_like(before, -1.0), (0, 0) if k % 4 < 2 else (60, 4)))
+    torch.cuda.synchronize()
+    got = [sa.paged_decode(c.cache, q, *see, scores=work, stream=s) if k % 3 else
+           sa.paged_decode(c.cache, q, *see, scores=work, scores_out=out, stream=s, keep_tail=False)
+           for k, (c, q, s, _, work, out, see) in enumerate(calls)]
+    torch.cuda.synchronize()
+    for k, ((c, q, _, before, work, out, see), (o, lse)) in enumerate(zip(calls, got)):
+        after = work if k % 3 else out
+        check_decode(c, q, o, lse, *see, None, before, after)
+        for s, n in enumerate(c.lens):
+            assert torch.equal(after[s, :, n:], before[s, :, n:])
+
+
+def test_evictions_and_appends_on_two_streams_do_not_meet(sa):
+    cs = [Case(sa, 360 + i, [300, 80 + i], 2, 64, 16) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    scores = [c.scores() for c in cs]
+    host = [s.cpu().numpy() for s in scores]
+    rows = [[c.read(c.table_np, s, n) for s, n in enumerate(c.lens)] for c in cs]
+    new = [new_rows(c, 2, "bf16", i) for i, c in enumerate(cs)]
+    torch.cuda.synchronize()
+    keeps = []
+    for budget in (70, 40):
+        for c, w, s in zip(cs, scores, streams):
+            keeps.append(sa.cache_evict(c.cache, w, budget, 2, 5, stream=s))
+    for c, (kn, vn), w, s in zip(cs, new, scores, streams):
+        sa.paged_append(c.cache, kn, vn, scores=w, stream=s)  # over the last position
+    torch.cuda.synchronize()
+    for i, c in enumerate(cs):
+        for s, n in enumerate(c.lens):
+            got = c.read(c.table_np, s, 40)
+            for h in range(2):
+                a = Pg.keep_one(host[i][s, h], n, 70, 2, 5)
+                b = Pg.keep_one(host[i][s, h][a], 70, 40, 2, 5)
+                assert keeps[i][s, h].tolist() == a.tolist() and keeps[2 + i][s, h].tolist() == b.tolist()
+                for x in range(2):
+                    want = rows[i][s][x][h][a[b]]
+                    want[39] = new[i][x][s, h].view(torch.int16).cpu().numpy()
+                    np.testing.assert_array_equal(got[x][h], want)
+                left = host[i][s, h][a[b]].copy()
+                left[39] = 0
+                np.testing.assert_array_equal(scores[i][s, h, :40].cpu().numpy(), left)
