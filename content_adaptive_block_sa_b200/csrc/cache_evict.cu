@@ -24,6 +24,7 @@
 // them 167 the movement at the rate of a copy and 22 the selection; one sequence
 // of 8192 to 2048: 13 us, the selection's barriers and the chain position -> page
 // -> row; 48 e4m3 sequences of 700..16000 to 1000: 29 us.
+// In place, where one block moves a slice of a row's columns in order: 408, 22, 36.
 #include <cooperative_groups.h>
 #include <math.h>
 

@@ -13,7 +13,9 @@ inline int dtype_bytes(int dtype) { return dtype == SA_DTYPE_E4M3 ? 1 : dtype ==
 // Location codes of the status word.
 enum { kWherePagedLen = 700, kWherePagedPage = 701, kWherePagedRange = 702 };
 
-// Quotient by a fixed divisor for 0 <= n < 2^31: (mulhi(m, n) + n) >> sh.
+// Quotient by a fixed divisor for 0 <= n < 2^31: (mulhi(m, n) + n) >> sh, by
+// Granlund and Montgomery's method for invariant divisors (1994); n's bound keeps
+// the sum within 32 bits.
 struct Divisor {
   uint32_t m = 1;
   int sh = 0;

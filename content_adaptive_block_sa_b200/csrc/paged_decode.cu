@@ -25,12 +25,14 @@
 // multiplies its own 16 keys without waiting for others, and at 8 columns the
 // products keep the tensor pipe 15% busy while memory runs at the rate of a copy.
 //
-// Measured (B200; device time): 16 sequences of 65537..131072 positions, 32 query
-// and 8 key/value heads, bf16: 844 us, 7.3 TB/s; one of 131072: 88 us, 6.1 TB/s;
-// one of 1777: 8.3 us, bound by the two kernels' start and the chain length ->
+// Measured (B200; calls in a graph): 16 sequences of 65537..131072 positions, 32
+// query and 8 key/value heads, bf16: 852 us, 7.2 TB/s; one of 131072: 90 us, 6.0
+// TB/s; one of 1777: 8.3 us, bound by the two kernels' start and the chain length ->
 // page -> row -> products -> join; 24 e4m3 sequences of up to 32768, 64 / 8 heads:
-// 122 us, 6.2 TB/s; 96 fp16 sequences of 3..2048, 12 / 12 heads of 64: 58 us, 5.3
+// 122 us, 6.2 TB/s; 96 fp16 sequences of 3..2048, 12 / 12 heads of 64: 59 us, 5.3
 // TB/s. About 7 us of every call are its start, its join and the SMs' unequal ends.
+// More than 16 query heads a key/value head read its keys and values once for every
+// 16 (8 sequences of 32768, 128 / 1 heads: 155 us).
 // Tried and not kept: a worker per warp (no faster, four times the partial
 // results), three blocks an SM with two stages (e4m3 and long bf16 items 2 to 5%
 // slower), values loaded on their own after the keys (the look-ups double).
