@@ -636,7 +636,9 @@ sa_status sa_paged_decode_workspace_size(const sa_paged_cache* cache,
 /* O and LSE of one query token per sequence over its cache: with the visible
  * positions j of sequence s, x_hj = q_h . k_j * scale, LSE_h = log sum_j
  * exp(x_hj), O_h = sum_j exp(x_hj - LSE_h) v_j. A sequence of length 0 gets
- * O = 0 and LSE = -inf.
+ * O = 0 and LSE = -inf. What stands in slots that are not visible does not
+ * matter; an infinite v_j that is visible makes its elements of O inf or NaN
+ * (weights are multiplied as sums of two 16-bit numbers, of which one may be 0).
  *  q [n_seq, Hq, d], o [n_seq, Hq, d] (not over q), lse fp32 [n_seq, Hq] dense.
  *  scores_in, scores_out  with `accumulate`: DEVICE fp32 [n_seq, Hkv, >=
  *              capacity]; scores_out[s, g, j] = scores_in[s, g, j] + sum of
@@ -680,7 +682,7 @@ sa_status sa_cache_evict_workspace_size(const sa_paged_cache* cache, const sa_ev
  *              sa_paged_decode.
  *  dst_table   DEVICE int32 [n_seq, dst_max_pages]: pages of the same pools that
  *              receive the rows; none of them may hold positions of the cache
- *              itself. NULL: the cache's own pages, in place (then no two
+ *              itself or stand in the table twice. NULL: the cache's own pages, in place (then no two
  *              sequences may share a page).
  *  keep        DEVICE int32 [n_seq, Hkv, budget] out: the kept positions,
  *              ascending, -1 padded.
